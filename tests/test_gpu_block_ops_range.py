@@ -1,0 +1,40 @@
+"""The operators around the linears at the ends of their ranges: exponents that leave fp32, heads whose squares do, one-row
+views, calls whose operands do not belong together."""
+import pytest
+import torch
+
+from epilogue_gemm_nvfp4_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Mq,Mk,H", [(3, 900, 2), (200, 130, 1), (3000, 400, 8)])
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 28, 1.0e30, 1.0e36, 1.0e38])
+def test_attention_to_the_largest_scores_alone(D, Mq, Mk, H, scale):
+    """Scores that are whole numbers (exact in fp32) times a scale that leaves the largest of them alone: the output is the
+    mean of v over the keys that share the largest score, which lie in different key tiles, and lse is that score plus the
+    logarithm of their number.  Tolerance: half a bf16 step of the result; half a bf16 step of each p (one that comes from a
+    product of score and scale below 2^24 is 1 only up to the rounding of that product, and the sum is of the unrounded p);
+    their number (at most 2^10) times 2^-23 of mean |v| for the sum, 2^-20 for the reciprocal and the merge of a cluster;
+    lse: 2^-21 of it for five roundings, 2^-20 for the logarithm."""
+    gen = torch.Generator(device="cuda").manual_seed(D + Mq)
+    q = torch.randint(-1, 2, (1, Mq, H, D), device="cuda", generator=gen).bfloat16()
+    k = torch.randint(-1, 2, (1, Mk, H, D), device="cuda", generator=gen).bfloat16()
+    k[:, Mk // 2:Mk // 2 * 2] = k[:, :Mk // 2]
+    q[:, 1], k[:, :, H - 1] = 1, -k[:, :, H - 1].abs()  # rows without a positive score, one of small ones only
+    v = torch.randn(1, Mk, H, D, device="cuda", generator=gen).bfloat16()
+    out, lse = B.cross_attention(q, k, v, scale=scale, want_lse=True)
+    B.check_device_error()
+    s = torch.einsum("bqhd,bkhd->bhqk", q.double(), k.double())
+    top = s.amax(-1, keepdim=True)
+    w = (s == top).double()
+    count = w.sum(-1, keepdim=True)
+    assert count.max() <= 1024
+    want = torch.einsum("bhqk,bkhd->bqhd", w / count, v.double())
+    mag = torch.einsum("bhqk,bkhd->bqhd", w / count, v.double().abs())
+    room = want.abs() * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -13 + 2.0 ** -20) * (1 + 2.0 ** -8)
+    assert ((out.double() - want).abs() <= room).all()
+    if scale < 1.0e37:  # the logarithm itself fits fp32
+        ref = (top * scale + count.log())[..., 0]
+        assert ((lse.double() - ref).abs() <= ref.abs() * 2.0 ** -21 + 2.0 ** -20).all()
