@@ -52,6 +52,29 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
+// Both elements times 2^-70.
+__device__ __forceinline__ uint32_t down70(uint32_t w) {
+  const float2 x = bf16x2_to_float2(w);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(x.x * 0x1p-70f, x.y * 0x1p-70f);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The sum of squares of a head from this lane's 8 elements of it, in each of the head's lanes.
+template <int kLanes>
+__device__ __forceinline__ float head_squares(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = bf16x2_to_float2(w[j]);
+    s2 = fma2(x, x, s2);
+  }
+  float ss = s2.x + s2.y;
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+  return ss;
+}
+
 template <int D, bool kInterleaved>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
@@ -134,40 +157,50 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeArgs a) {
     }
   }
 
+  // this lane's part of one head, from its 8 elements; every lane of the warp is here (partners' elements)
+  auto turn = [&](uint4 u, float rstd) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t p;
+      if constexpr (kInterleaved) {
+        p = __byte_perm(w[j], 0u, 0x1032);
+      } else {
+        p = __shfl_sync(0xFFFFFFFFu, w[j], src);
+      }
+      p = turned ? p : 0u;  // an unturned element takes nothing, not even 0 * infinity, from another
+      const float2 y = fma2(bf16x2_to_float2(p), make_float2(Bm[2 * j], Bm[2 * j + 1]),
+                            mul2(bf16x2_to_float2(w[j]), make_float2(A[2 * j], A[2 * j + 1])));
+      const float2 z = mul2(y, make_float2(rstd, rstd));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(z.x, z.y);
+      r[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+  };
   while (true) {
+    uint32_t wide = 0u;  // steps whose head's squares leave fp32 (elements from about 1e18 on)
 #pragma unroll
     for (int i = 0; i < kRopeFlight; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      float2 rstd = make_float2(1.0f, 1.0f);
+      float rstd = 1.0f;
       if (h.gamma) {
-        float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = bf16x2_to_float2(w[j]);
-          s2 = fma2(x, x, s2);
-        }
-        float ss = s2.x + s2.y;
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        rstd.x = rstd.y = rsqrtf(__fmaf_rn(ss, 1.0f / D, a.eps));
+        rstd = rsqrtf(__fmaf_rn(head_squares<kLanes>(v[i]), 1.0f / D, a.eps));
+        if (!(rstd > 0.0f)) wide |= 1u << i;
       }
-      uint32_t r[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t p;
-        if constexpr (kInterleaved) {
-          p = __byte_perm(w[j], 0u, 0x1032);
-        } else {
-          p = __shfl_sync(0xFFFFFFFFu, w[j], src);
-        }
-        p = turned ? p : 0u;  // an unturned element takes nothing, not even 0 * infinity, from another
-        const float2 y = fma2(bf16x2_to_float2(p), make_float2(Bm[2 * j], Bm[2 * j + 1]),
-                              mul2(bf16x2_to_float2(w[j]), make_float2(A[2 * j], A[2 * j + 1])));
-        const float2 z = mul2(y, rstd);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(z.x, z.y);
-        r[j] = *reinterpret_cast<const uint32_t*>(&b);
+      const uint4 r = turn(v[i], rstd);
+      if (rstd > 0.0f && head + i * kHeads < head_end) *reinterpret_cast<uint4*>(op + i * o_step) = r;
+    }
+    if (__any_sync(0xFFFFFFFFu, wide != 0u)) {
+      // those, not written yet: read again and taken down by 2^70, beside which eps is nothing
+#pragma unroll 1
+      for (int i = 0; i < kRopeFlight; ++i) {
+        const bool mine = (wide >> i & 1u) != 0u && head + i * kHeads < head_end;
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (mine) u = *reinterpret_cast<const uint4*>(xp + i * x_step);
+        u = make_uint4(down70(u.x), down70(u.y), down70(u.z), down70(u.w));
+        const uint4 r = turn(u, rsqrtf(head_squares<kLanes>(u) * (1.0f / D)));
+        if (mine) *reinterpret_cast<uint4*>(op + i * o_step) = r;
       }
-      if (head + i * kHeads < head_end) *reinterpret_cast<uint4*>(op + i * o_step) = make_uint4(r[0], r[1], r[2], r[3]);
     }
     head += kRopeFlight * kHeads;
     if (head - lane / kLanes >= head_end) break;  // warp-uniform

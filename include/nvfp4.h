@@ -373,7 +373,7 @@ typedef struct {
  * between the QKV product and attention:
  *   y = x / sqrt(mean_d(x^2) + eps) * gamma per head (y = x without gamma), then for each pair (a, b)
  *   out[a] = y[a] * cos - y[b] * sin,  out[b] = y[b] * cos + y[a] * sin,
- * in fp32, rounded once to bf16.
+ * in fp32, rounded once to bf16; a head whose sum of squares leaves fp32 is normed at a scale where it does not.
  * Rules: head_dim 64, 128 or 256; x, out, gamma, cos and sin 16-byte aligned; strides of x and out
  * multiples of 8 elements; head strides, and out's row stride when rows > 1, >= head_dim (x's row stride may be
  * 0); ld_table a multiple of 4 and >= rot_dim / 2; rows

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from epilogue_gemm_nvfp4_b200 import binding as B
+from tests import test_gpu_norm_rope as norm_rope
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,32 @@ def test_attention_to_the_largest_scores_alone(D, Mq, Mk, H, scale):
     if scale < 1.0e37:  # the logarithm itself fits fp32
         ref = (top * scale + count.log())[..., 0]
         assert ((lse.double() - ref).abs() <= ref.abs() * 2.0 ** -21 + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rows", [9, 4000])
+def test_head_norm_of_heads_whose_squares_leave_fp32(D, interleaved, rows):
+    """Heads of ordinary size beside heads of up to bf16's largest value (and of a few such elements), with a gamma that takes
+    element times gamma past fp32 as well.  The formula and its tolerance are those of the operator's tests."""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    x = torch.randn(rows, 5, D, device="cuda", generator=gen)
+    x[1::3, 1] *= 2.0 ** 100
+    x[2::3, 2] = x[2::3, 2].clamp(-3, 3) * 2.0 ** 126
+    x[::4, 3, ::9] *= 2.0 ** 80   # the others vanish beside these, but are not zero
+    x = x.bfloat16()
+    assert x.isfinite().all()
+    cos, sin = norm_rope.table(rows, D // 2)
+    gamma = (torch.rand(D, device="cuda", generator=gen) * 8 - 4).bfloat16()
+    out, _ = B.qk_norm_rope(x, None, cos, sin, gamma_q=gamma, interleaved=interleaved)
+    some = slice(0, rows) if rows < 100 else slice(1990, 2010)
+    ref = norm_rope.reference(x[some], gamma, cos[some], sin[some], None, interleaved, 1e-6)
+    norm_rope.assert_close(out[some], ref)
+    # an infinity makes its head's other elements zeros and itself NaN; the heads beside it keep their bits
+    y = x.clone()
+    y[4, 1, 3] = float("inf")
+    got = B.qk_norm_rope(y, None, None, None, gamma_q=gamma)[0]
+    want = B.qk_norm_rope(x, None, None, None, gamma_q=gamma)[0]
+    assert got[4, 1, 3].isnan() and (got[4, 1, :3] == 0).all() and (got[4, 1, 4:] == 0).all()
+    got[4, 1] = want[4, 1]
+    assert torch.equal(got, want)
