@@ -152,6 +152,8 @@ uint64_t wait_timeout_ns() {
 #ifdef NVFP4_TEST_HOOKS
 // Test builds only (libnvfp4_testhooks.so): see nvfp4_test_withhold_split_ready.
 std::atomic<int> g_test_withhold_split_ready{0};
+// The same for the operators around the linears: see nvfp4_test_withhold_arrivals.
+std::atomic<int> g_test_withhold_arrivals{0};
 #endif
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -550,6 +552,9 @@ size_t nvfp4_linear_noalloc_scratch_bytes(void) { return kNoAllocScratchBytes; }
 // out, the kernel gives up and nvfp4_get_device_error reports NVFP4_ERR_DEVICE_TIMEOUT.  This is how the
 // device-timeout path is exercised without faulting or hanging anything.
 NVFP4_API void nvfp4_test_withhold_split_ready(int32_t on) { g_test_withhold_split_ready.store(on != 0); }
+// While `on` is non-zero, a few-row linear launched afterwards never gives an accumulator back, so that its MMA warp's wait for a
+// free one runs out after the producer has issued its last load.
+NVFP4_API void nvfp4_test_withhold_arrivals(int32_t on) { g_test_withhold_arrivals.store(on != 0); }
 #endif
 
 nvfp4_status nvfp4_get_device_error(nvfp4_stream_t stream) {

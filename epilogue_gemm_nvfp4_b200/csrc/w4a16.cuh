@@ -82,6 +82,9 @@ struct W4Args {
   int kind;
   unsigned int* error_word;
   uint64_t timeout_ns;
+#ifdef NVFP4_TEST_HOOKS
+  int test_withhold;  // test builds only: accumulators are never given back, so the wait for the next free one runs out
+#endif
 };
 
 // Columns of the digit operand for MP rows, and the bytes of one chunk image: the columns' codes (128 bytes each, in
@@ -436,12 +439,11 @@ __global__ void __launch_bounds__(640, 1)  // 96 registers for its 384 threads: 
           phase ^= 1u;
         }
       }
-      if (!ok) {
-        raise_device_error(a.error_word, kErrTimeout, abort_flag);
-        // the copies in flight write this CTA's shared memory: wait for them before it ends
-        for (int i = max(0, n - C::STAGES); i < n; ++i)
-          mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, a.timeout_ns);
-      }
+      if (!ok) raise_device_error(a.error_word, kErrTimeout, abort_flag);
+      // The copies in flight write this CTA's shared memory: wait for them before it ends.  Whatever became of the others:
+      // the MMA warp, which waits for the same copies, may have given up.
+      for (int i = max(0, n - C::STAGES); i < n; ++i)
+        if (!mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, a.timeout_ns)) break;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -555,7 +557,11 @@ __global__ void __launch_bounds__(640, 1)  // 96 registers for its 384 threads: 
       }
       tc_fence_before();
       __syncwarp();
+#ifdef NVFP4_TEST_HOOKS
+      if (lane == 0 && !a.test_withhold) mbar_arrive(&acc_empty[buf]);
+#else
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
+#endif
       if (++buf == C::BUFS) {
         buf = 0;
         acc_phase ^= 1u;

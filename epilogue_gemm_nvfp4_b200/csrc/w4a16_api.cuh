@@ -152,6 +152,9 @@ nvfp4_status nvfp4_w4a16_linear(const void* x, int64_t M, int64_t ldx, int32_t s
   a.kind = epi->kind;
   a.error_word = st->error_word;
   a.timeout_ns = wait_timeout_ns();
+#ifdef NVFP4_TEST_HOOKS
+  a.test_withhold = g_test_withhold_arrivals.load();
+#endif
   CUtensorMap map;
   if (nvfp4_status e = make_code_map(&map, w)) return e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
