@@ -103,6 +103,9 @@ struct AttnArgs {
   int heads;
   unsigned int* error_word;
   uint64_t timeout_ns;
+#ifdef NVFP4_TEST_HOOKS
+  int test_withhold;  // test builds only: the probabilities are never handed over, so the wait for them runs out
+#endif
 };
 
 struct AttnMaps {
@@ -212,13 +215,12 @@ __global__ void __launch_bounds__(384, 1)
           ++n;
         }
       }
-      if (!ok) {
-        raise_device_error(args.error_word, kErrTimeout, abort_flag);
-        // the copies in flight write this CTA's shared memory: wait for them before it ends
-        mbar_wait(q_full, 0, never_abort, args.timeout_ns);
-        for (int i = max(0, n - C::STAGES); i < n; ++i)
-          mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, args.timeout_ns);
-      }
+      if (!ok) raise_device_error(args.error_word, kErrTimeout, abort_flag);
+      // The copies in flight write this CTA's shared memory: wait for them before it ends.  Whatever became of the others:
+      // the MMA warp, which waits for the same copies, may have given up.
+      bool landed = mbar_wait(q_full, 0, never_abort, args.timeout_ns);
+      for (int i = max(0, n - C::STAGES); landed && i < n; ++i)
+        landed = mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, args.timeout_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -374,6 +376,9 @@ __global__ void __launch_bounds__(384, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
+#ifdef NVFP4_TEST_HOOKS
+      if (args.test_withhold) continue;
+#endif
       if (lane == 0) mbar_arrive(&p_ready[j & 1]);
     }
     // P V of the last tile but one may still run (its S was issued before it), and a wait for a parity tells the last
@@ -671,13 +676,11 @@ __global__ void __launch_bounds__(384, 1)
             if (!C::K_FIRST && t + 1 < wk.tiles) load_k(t + 1);
           }
         }
-        if (!ok) {
-          raise_device_error(args.error_word, kErrTimeout, abort_flag);
-          // the copies in flight write this CTA's shared memory: wait for them before it ends
-          if (w > 0) mbar_wait(q_full, (w - 1) & 1, never_abort, args.timeout_ns);
-          for (int i = max(0, n - C::STAGES); i < n; ++i)
-            mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, args.timeout_ns);
-        }
+        if (!ok) raise_device_error(args.error_word, kErrTimeout, abort_flag);
+        // the copies in flight, as above
+        bool landed = w == 0 || mbar_wait(q_full, (w - 1) & 1, never_abort, args.timeout_ns);
+        for (int i = max(0, n - C::STAGES); landed && i < n; ++i)
+          landed = mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, args.timeout_ns);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -887,6 +890,9 @@ __global__ void __launch_bounds__(384, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
+#ifdef NVFP4_TEST_HOOKS
+        if (args.test_withhold) continue;
+#endif
         if (lane == 0) mbar_arrive(&p_ready[q]);
       }
       chunk0 += 2 * T * C::CHUNKS;
@@ -1115,17 +1121,17 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
             load_v(t);
           }
         }
-        if (!ok) {
-          raise_device_error(args.error_word, kErrTimeout, abort_flag);
-          // the copies in flight write this CTA's shared memory: wait for them before it ends
-          // (rank 1's are counted by the leader, which waits here for both CTAs' before the cluster's last barrier)
-          if (rank == 0) {
-            if (w > 0) mbar_wait(q_full, (w - 1) & 1, never_abort, args.timeout_ns);
-            for (int i = max(0, n - C::STAGES); i < n; ++i)
-              mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, args.timeout_ns);
-          } else {
-            for (int i = max(0, z - 2); i < z; ++i) mbar_wait(&v_own[i & 1], (i >> 1) & 1, never_abort, args.timeout_ns);
-          }
+        if (!ok) raise_device_error(args.error_word, kErrTimeout, abort_flag);
+        // The copies in flight, as above.  Rank 1's are counted by the leader, which waits here for both CTAs' before the
+        // cluster's last barrier; where it gave up before rank 1 did, those of rank 1 that it never armed a barrier
+        // for have a whole time limit to land.
+        if (rank == 0) {
+          bool landed = w == 0 || mbar_wait(q_full, (w - 1) & 1, never_abort, args.timeout_ns);
+          for (int i = max(0, n - C::STAGES); landed && i < n; ++i)
+            landed = mbar_wait(&full[i % C::STAGES], (i / C::STAGES) & 1, never_abort, args.timeout_ns);
+          if (!ok && landed) mbar_wait(&full[n % C::STAGES], (n / C::STAGES) & 1, never_abort, args.timeout_ns);
+        } else {
+          for (int i = max(0, z - 2); i < z; ++i) mbar_wait(&v_own[i & 1], (i >> 1) & 1, never_abort, args.timeout_ns);
         }
       }
       __syncwarp();
@@ -1316,6 +1322,9 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
+#ifdef NVFP4_TEST_HOOKS
+        if (args.test_withhold) continue;
+#endif
         if (lane == 0) {
           if (clears) mbar_arrive_release_cluster(leader_p[buf]);
           else mbar_arrive_cluster(leader_p[buf]);

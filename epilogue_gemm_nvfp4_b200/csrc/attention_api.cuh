@@ -202,6 +202,9 @@ nvfp4_status nvfp4_cross_attention(const nvfp4_attention_desc* d, nvfp4_stream_t
   a.heads = d->heads;
   a.error_word = st->error_word;
   a.timeout_ns = wait_timeout_ns();
+#ifdef NVFP4_TEST_HOOKS
+  a.test_withhold = g_test_withhold_arrivals.load();
+#endif
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Tiles of 128 rows, one per CTA with the keys split over clusters while there is room; or the persistent kernels' pieces
   // of two tiles.  The latter need less time for two tiles than the former for two in turn, but more than for one:

@@ -552,8 +552,8 @@ size_t nvfp4_linear_noalloc_scratch_bytes(void) { return kNoAllocScratchBytes; }
 // out, the kernel gives up and nvfp4_get_device_error reports NVFP4_ERR_DEVICE_TIMEOUT.  This is how the
 // device-timeout path is exercised without faulting or hanging anything.
 NVFP4_API void nvfp4_test_withhold_split_ready(int32_t on) { g_test_withhold_split_ready.store(on != 0); }
-// While `on` is non-zero, a few-row linear launched afterwards never gives an accumulator back, so that its MMA warp's wait for a
-// free one runs out after the producer has issued its last load.
+// While `on` is non-zero, a few-row linear launched afterwards never gives an accumulator back, and an attention never hands its
+// probabilities over, so that the MMA warp's wait for them runs out, where it can after the producer's last load.
 NVFP4_API void nvfp4_test_withhold_arrivals(int32_t on) { g_test_withhold_arrivals.store(on != 0); }
 #endif
 

@@ -68,3 +68,21 @@ for M in (1, 3, 12, 32):   # digits made in the product kernel's own CTAs, and b
 
 def test_few_row_linear_reports_a_wait_that_runs_out(tmp_path):
     run(tmp_path, W4A16, ["rows1", "rows3", "rows12", "rows32"])
+
+
+ATTENTION = r"""
+lens = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+r = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+for D in (64, 128, 256):
+    # tiles, alone and split over a cluster; pieces of two tiles, more than one per CTA or pair; keys whose loads are all out at
+    # once and keys that go round the ring; lengths that end inside a tile (V rows cleared), and none
+    for name, B_, Mq, Mk, H, n in (("tile", 1, 64, 128, 1, None), ("split", 1, 3, 1300, 2, None), ("pieces", 2, 3000, 128, 8, None),
+                                   ("ring", 2, 3000, 900, 8, (900, 333)), ("none", 3, 2000, 200, 8, (0, 200, 7))):
+        q, k, v = r(B_, Mq, H, D), r(B_, Mk, H, D), r(B_, Mk, H, D)
+        n = n and lens(*n)
+        check(f"{name}{D}", lambda: B.cross_attention(q, k, v, kv_lens=n))
+"""
+
+
+def test_attention_reports_a_wait_that_runs_out(tmp_path):
+    run(tmp_path, ATTENTION, [f"{name}{D}" for D in (64, 128, 256) for name in ("tile", "split", "pieces", "ring", "none")])
