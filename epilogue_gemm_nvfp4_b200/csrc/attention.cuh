@@ -1149,6 +1149,11 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
           tc_fence_after();
           return got;
         };
+        auto wait_cluster = [&](uint64_t* bar, uint32_t parity) {
+          const bool got = __all_sync(0xFFFFFFFFu, mbar_wait<true>(bar, parity, abort_flag, args.timeout_ns));
+          tc_fence_after();
+          return got;
+        };
         auto advance = [&] {
           tc_commit_pair_warp(&empty[st], 0x3);
           if (++st == C::STAGES) {
@@ -1196,7 +1201,9 @@ __global__ void __launch_bounds__(384, 1) __cluster_dims__(2, 1, 1)
               if (j + 2 == wk.tiles) tc_commit_pair_warp(q_empty, 0x3);
             }
             if (ok && j == 0) ok = wait(o_free, (w & 1) ^ 1);
-            ok = ok && wait(&p_ready[n & 1], (n >> 1) & 1) && issue_o(n & 1, j);
+            // rank 1's arrivals for a tile whose V rows it cleared publish those zeros, which these MMAs read
+            ok = ok && (attn_clears(args, wk, j) ? wait_cluster(&p_ready[n & 1], (n >> 1) & 1) : wait(&p_ready[n & 1], (n >> 1) & 1)) &&
+                 issue_o(n & 1, j);
           }
           ++w;
         }

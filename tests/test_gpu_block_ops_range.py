@@ -68,3 +68,21 @@ def test_head_norm_of_heads_whose_squares_leave_fp32(D, interleaved, rows):
     assert got[4, 1, 3].isnan() and (got[4, 1, :3] == 0).all() and (got[4, 1, 4:] == 0).all()
     got[4, 1] = want[4, 1]
     assert torch.equal(got, want)
+
+
+def test_cleared_rows_of_every_last_tile():
+    """Head_dim 256 on CTA pairs, thousands of pieces of work of one to three key tiles, each of which ends inside a tile with NaN
+    and infinities behind it: every piece's zeros reach the other CTA's products, in many repeats."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()
+    Bn, Mq, Mk, H, D = 24, 1100, 384, 24, 256
+    q, k, v = r(Bn, Mq, H, D), r(Bn, Mk, H, D), r(Bn, Mk, H, D)
+    n = torch.randint(1, Mk, (Bn,), device="cuda", generator=gen, dtype=torch.int32)
+    gone = (torch.arange(Mk, device="cuda") >= n[:, None])[:, :, None, None]
+    clean = B.cross_attention(q, torch.where(gone, 0, k), torch.where(gone, 0, v), kv_lens=n)
+    k, v = torch.where(gone, float("nan"), k), torch.where(gone, float("inf"), v)
+    out = torch.empty_like(q)
+    for _ in range(50):
+        B.cross_attention(q, k, v, kv_lens=n, out=out)
+        assert torch.equal(out, clean)
+    B.check_device_error()
