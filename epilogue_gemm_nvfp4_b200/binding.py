@@ -363,6 +363,8 @@ def _here(stream, t: torch.Tensor):
     if not t.is_cuda:
         raise ValueError("the call's tensors are CUDA tensors")
     if stream is not None:
+        if stream.device.index != t.get_device():
+            raise ValueError(f"stream: of {stream.device}, the call's tensors are on cuda:{t.get_device()}")
         return torch.cuda.stream(stream)
     if t.get_device() != _current_device():
         return torch.cuda.device(t.device)
