@@ -433,7 +433,7 @@ def w4a16_linear(x: torch.Tensor, w: QTensor, kind: str = "bias", bias=None, sil
 
 def _ld(t: torch.Tensor) -> int:
     """Row stride of a matrix; its width where there is one row, whose stride says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _heads(x: torch.Tensor, out: torch.Tensor, gamma) -> CHeads:

@@ -10,10 +10,10 @@ namespace {
 nvfp4_status check_heads(const nvfp4_heads* h, int64_t rows, int32_t head_dim, float eps) {
   if ((rows > 0 && (!h->x || !h->out)) || h->heads <= 0) return NVFP4_ERR_INVALID_ARG;
   if (h->heads > 1 && (h->head_stride < head_dim || h->out_head_stride < head_dim)) return NVFP4_ERR_INVALID_ARG;
-  if (h->row_stride < 0 || (rows > 1 && h->out_row_stride < head_dim)) return NVFP4_ERR_INVALID_ARG;
+  if (rows > 1 && (h->row_stride < 0 || h->out_row_stride < head_dim)) return NVFP4_ERR_INVALID_ARG;
   if (h->heads > 65535) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (h->gamma && !(eps > 0.0f && eps < 3.0e38f)) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned16(h->x) || !aligned16(h->out) || h->row_stride % 8 || h->out_row_stride % 8 ||
+  if (!aligned16(h->x) || !aligned16(h->out) || (rows > 1 && (h->row_stride % 8 || h->out_row_stride % 8)) ||
       (h->heads > 1 && (h->head_stride % 8 || h->out_head_stride % 8)) || (h->gamma && !aligned16(h->gamma)))
     return NVFP4_ERR_MISALIGNED;
   return NVFP4_OK;

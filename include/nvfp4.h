@@ -375,9 +375,9 @@ typedef struct {
  *   out[a] = y[a] * cos - y[b] * sin,  out[b] = y[b] * cos + y[a] * sin,
  * in fp32, rounded once to bf16; a head whose sum of squares leaves fp32 is normed at a scale where it does not.
  * Rules: head_dim 64, 128 or 256; x, out, gamma, cos and sin 16-byte aligned; strides of x and out
- * multiples of 8 elements; head strides, and out's row stride when rows > 1, >= head_dim (x's row stride may be
- * 0); ld_table a multiple of 4 and >= rot_dim / 2; rows
- * times the head chunks (of 1536 elements) of q and k at most 2^31.  rows == 0 writes nothing.
+ * multiples of 8 elements; head strides, and out's row stride, >= head_dim (x's row stride may be
+ * 0); the row strides of a single row and the head strides of a single head are not read; ld_table a multiple of 4
+ * and >= rot_dim / 2; rows times the head chunks (of 1536 elements) of q and k at most 2^31.  rows == 0 writes nothing.
  */
 NVFP4_API nvfp4_status nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, int64_t rows, int32_t head_dim,
                                           const nvfp4_rope_desc* rope, nvfp4_stream_t stream);

@@ -86,3 +86,29 @@ def test_cleared_rows_of_every_last_tile():
         B.cross_attention(q, k, v, kv_lens=n, out=out)
         assert torch.equal(out, clean)
     B.check_device_error()
+
+
+def test_one_row_of_a_buffer_with_any_row_stride():
+    """A single row's stride says nothing: rows of buffers whose stride no kernel could take give the contiguous row's bits."""
+    K, N, D = 256, 96, 128
+    w = B.quantize(torch.randn(N, K, device="cuda").bfloat16())
+
+    def row(*shape, dtype=torch.bfloat16, extra=1):
+        """The first of three rows of a buffer whose rows are `extra` elements longer."""
+        n = shape[0] * shape[1] if len(shape) == 2 else shape[0]
+        inner = (shape[1], 1) if len(shape) == 2 else (1,)
+        return torch.randn(3, n + extra, device="cuda").to(dtype).as_strided((1, *shape), (n + extra, *inner))
+
+    def plain(t):
+        return torch.empty(t.shape, dtype=t.dtype, device="cuda").copy_(t)
+
+    x, res, gate, out = row(K), row(N), torch.rand(N, device="cuda"), row(N, extra=3)
+    assert x.stride(0) == K + 1
+    B.w4a16_linear(x, w, "resid_gate", residual=res, gate=gate, out=out)
+    assert torch.equal(out, B.w4a16_linear(plain(x), w, "resid_gate", residual=plain(res), gate=gate))
+    q, k, out = row(4, D), row(2, D), row(4, D, extra=5)
+    cos, sin = row(D // 2, dtype=torch.float32), row(D // 2, dtype=torch.float32, extra=3)
+    qo, ko = B.qk_norm_rope(q, k, cos, sin, q_out=out)
+    qc, kc = B.qk_norm_rope(plain(q), plain(k), plain(cos), plain(sin))
+    assert torch.equal(qo, qc) and torch.equal(ko, kc)
+    assert torch.equal(B.cross_attention(q[None], k[None], k[None]), B.cross_attention(plain(q)[None], plain(k)[None], plain(k)[None]))
