@@ -466,7 +466,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor | No
     else:
         _require(q_out, "q_out", torch.bfloat16, dev, q.shape)
     hk = None
-    if k is not None:
+    if k is None:
+        if k_out is not None or gamma_k is not None:
+            raise ValueError("k_out and gamma_k belong to k")
+    else:
         if k.dim() != 3 or k.shape[0] != rows or k.shape[2] != D:
             raise ValueError("q and k: [rows, heads, head_dim] with the same rows and head_dim")
         _require(k, "k", torch.bfloat16, dev)
@@ -480,6 +483,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor | No
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     if cos is None:
+        if positions is not None:
+            raise ValueError("positions belong to cos and sin")
         rope = CRope(None, None, 0, 0, 0, 0, None, eps)
     else:
         _require(cos, "cos", torch.float32, dev)

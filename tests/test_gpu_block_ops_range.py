@@ -112,3 +112,12 @@ def test_one_row_of_a_buffer_with_any_row_stride():
     qc, kc = B.qk_norm_rope(plain(q), plain(k), plain(cos), plain(sin))
     assert torch.equal(qo, qc) and torch.equal(ko, kc)
     assert torch.equal(B.cross_attention(q[None], k[None], k[None]), B.cross_attention(plain(q)[None], plain(k)[None], plain(k)[None]))
+
+
+def test_head_norm_refuses_operands_of_what_is_not_there():
+    """An output for no k would come back unwritten; positions without tables would turn nothing."""
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    pos, gamma = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(k_out=torch.empty_like(q)), dict(gamma_k=gamma), dict(positions=pos)):
+        with pytest.raises(ValueError):
+            B.qk_norm_rope(q, None, None, None, **kw)
