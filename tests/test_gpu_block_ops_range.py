@@ -121,3 +121,15 @@ def test_head_norm_refuses_operands_of_what_is_not_there():
     for kw in (dict(k_out=torch.empty_like(q)), dict(gamma_k=gamma), dict(positions=pos)):
         with pytest.raises(ValueError):
             B.qk_norm_rope(q, None, None, None, **kw)
+
+
+def test_few_row_linear_refuses_a_weight_smaller_than_it_says():
+    """Codes or scale bytes of fewer rows or columns would be read past their end, and so would one row of codes for all."""
+    q = B.quantize(torch.randn(256, 128, device="cuda").bfloat16())
+    x = torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")
+    B.w4a16_linear(x, q)
+    for w in (B.QTensor(q.codes[:128], q.scales, q.g, 256, 128), B.QTensor(q.codes[:, :32], q.scales, q.g, 256, 128),
+              B.QTensor(q.codes[:1].expand(256, 64), q.scales, q.g, 256, 128), B.QTensor(q.codes, q.scales[:1024], q.g, 256, 128),
+              B.QTensor(q.codes.view(-1), q.scales, q.g, 256, 128), B.QTensor(q.codes, q.scales[::2], q.g, 256, 128)):
+        with pytest.raises(ValueError):
+            B.w4a16_linear(x, w)
