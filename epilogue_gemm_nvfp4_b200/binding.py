@@ -390,7 +390,8 @@ def _require(t, what, dtype, device, shape=None):
 def w4a16_linear(x: torch.Tensor, w: QTensor, kind: str = "bias", bias=None, silu_input: bool = False,
                  out: torch.Tensor | None = None, residual=None, gate=None, stream=None) -> torch.Tensor:
     """Linear of up to 32 bf16 rows on an NVFP4 weight through nvfp4_w4a16_linear: x (or silu(x) with
-    ``silu_input``) is not quantised.  ``kind`` is "bias", "gated_silu" or "resid_gate"."""
+    ``silu_input``) is rounded to 2^-17 of the largest of each 16 elements, not to NVFP4.  ``kind`` is "bias",
+    "gated_silu" or "resid_gate"."""
     here = _here(stream, x)
     if here is not None:
         with here:

@@ -1,4 +1,4 @@
-// The linear of a few rows on NVFP4 weights (W4A16): bf16 activations, not quantised, times a stored NVFP4
+// The linear of a few rows on NVFP4 weights (W4A16): bf16 activations, in block fixed point, times a stored NVFP4
 // weight.  For one to 32 rows the weight's 0.5625 bytes per element are nearly all that moves:
 //
 //   y[m,n] = g * sum_k x'[m,k] * e2m1(code[n,k]) * e4m3(scale[n, k/16]),   x' = x or silu(x)
@@ -12,9 +12,10 @@
 // element and E_m that of the row's.  (An integer q = rint(x' 2^16 / 2^e_b), |q| <= 2^17, in digits of -4 .. 4;
 // n / 2 has the E2M1 code |n|.)  The weight is the 128-row operand of tcgen05.mma.kind::mxf4nvf4, the digits
 // are its columns: digit t of row m is column t * MP + m, and the epilogue adds a row's columns with 8^-t.  Every
-// product is exact and summed in fp32; x' itself is exact for elements down to 2^-9 of their block's
-// largest, and off by at most 2^-17 of that one for smaller ones (2^-35 of the row's largest where a block
-// is below 2^-17 of it, the least E4M3 scale).  The rounding of the bf16 output is 2^-8.
+// product is exact and summed in fp32.  x' itself is rounded to at most 2^-17 of its block's power of two (2^-34 of the
+// row's where a block lies 2^-17 and more below it, the least E4M3 scale): nothing for bf16 elements down to 2^-9 of that
+// power, all of an element below 2^-17 of it; silu(x), an fp32 number, is rounded so throughout.  The rounding of
+// the bf16 output is 2^-8.
 // Measured: one row by [27648 x 4608] 17.1 us (4.2 TB/s of the weight's bytes), 7 rows by the gated [24576 x 4608] 18.5 us,
 // 32 rows by [4608 x 53248] 37.1 us (3.8 TB/s), 2 rows by [4608 x 256] 5.3 us.  About 5 us are launches, the first and the last
 // kernel.  The stream itself runs at HBM speed up to 16 rows; with 32 the digits (28 KB a chunk beside 36 KB of

@@ -300,7 +300,7 @@ NVFP4_API nvfp4_status nvfp4_int8_linear(const nvfp4_int8_tensor* a, const nvfp4
 
 /*
  * The linear of a few rows on a stored NVFP4 weight (W4A16): out = epilogue(x' x w^T) with bf16
- * activations that are not quantised, for the products of a DiT block that have one row per sample (the
+ * activations that are not quantised to NVFP4 (but see Arithmetic), for the products of a DiT block that have one row per sample (the
  * adaLN modulation vectors, the timestep's MLP) or a handful of tokens.
  *   y[m,n] = g * sum_k x'[m,k] * e2m1(code[n,k]) * e4m3(scale[n,k/16]),  fp32 accumulation;
  *   x' = x, or silu(x) = x / (1 + exp(-x)) when silu_input is non-zero (the activation in front of a
@@ -316,11 +316,14 @@ NVFP4_API nvfp4_status nvfp4_int8_linear(const nvfp4_int8_tensor* a, const nvfp4
  * scales and ld_codes 16-byte aligned; out, bias and residual aligned as their elements (any ld >= their
  * columns), gate 4-byte aligned.  Two or three launches, each of which starts while the
  * one before runs.
- * Arithmetic: x' is held as an 18-bit fixed-point number per 16-element block (elements 16 i .. 16 i + 15 of a
- * row): exact for elements down to 2^-9 of the block's largest, else with an absolute error of at most
- * 2^-17 of that one, or 2^-35 of the row's largest where that is more.  Its products with the weight are exact
- * and summed in fp32 in a fixed order.  A row with an infinity or a NaN gives NaN. A row of the
- * output is bitwise the same whatever rows accompany it.
+ * Arithmetic: x' is rounded to block fixed point: the 16 elements 16 i .. 16 i + 15 of a row become whole multiples of
+ * 2^-16 of the power of two of the largest of them (at least 2^-33 of that of the row's largest), so each is off
+ * by at most half of that, and an element below 2^-17 of its block's largest power of two becomes 0.  For x' = x,
+ * whose elements have 8 bits, this is exact for elements down to 2^-9 of that power.  silu(x), which has more bits, is
+ * rounded so in every element, on top of (|x| + 4) * 2^-22 of itself for the fast exponential and division (0 below
+ * x = -87).  The products with the weight are exact and summed in fp32 in a fixed order.  A row with an infinity or a
+ * NaN gives NaN.  A row of the output is bitwise the same whatever rows accompany it.
+ * residual may be out, with the same ld.
  */
 NVFP4_API size_t nvfp4_w4a16_workspace_bytes(int64_t M, int64_t N, int64_t K);
 NVFP4_API nvfp4_status nvfp4_w4a16_linear(const void* x, int64_t M, int64_t ldx, int32_t silu_input,

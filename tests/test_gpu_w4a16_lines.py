@@ -55,3 +55,30 @@ def test_the_residual_may_be_the_output():
         want = B.w4a16_linear(x, w, **more)
         got = B.w4a16_linear(x, w, **more, out=more["residual"])
         assert got.data_ptr() == more["residual"].data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [1, 6, 32])
+def test_silu_over_its_whole_range(M):
+    """silu(x) for x from -100 to 30, block by block, against the bound that the header states for x': 2^-17 of the power of two of the
+    block's largest (2^-34 of the row's), twice for an element that the first error takes to the other neighbour, (|x| + 4) 2^-22 of
+    itself, and 2^-119 where the division gives 0.  The weights are positive, so that every element's error would show."""
+    N, K = 64, 1024
+    w, value = make_weight(N, K, seed=3)
+    w.codes.bitwise_and_(0x77)
+    value = value.abs()
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    mid = torch.linspace(-97, 28, K // 16, device="cuda").repeat_interleave(16)
+    x = (mid + torch.randn(M, K, device="cuda", generator=gen)).bfloat16()
+    x[M // 2, 300:] = -90.5   # a row of the smallest values alone
+    x[M // 2, :300] = -60.0
+    xd = x.double()
+    s = xd / (1.0 + torch.exp(-xd))
+    power = lambda t: torch.exp2(torch.floor(torch.log2(t)))
+    block = torch.maximum(power(s.abs().view(M, -1, 16).amax(-1)), power(s.abs().amax(1, keepdim=True)) * 2.0 ** -17)
+    off = 2 * 2.0 ** -17 * block.repeat_interleave(16, dim=1) + s.abs() * (xd.abs() + 4) * 2.0 ** -22 + 2.0 ** -119
+    g = w.g.double()
+    ref = s @ value.t() * g
+    err = (off @ value.t() + (s.abs() @ value.t()) * (K / 8 + 12) * 2.0 ** -23) * g
+    out = B.w4a16_linear(x, w, silu_input=True)
+    B.check_device_error()
+    assert_within(out, ref, err + 2.0 ** -133)   # half of bf16's smallest step
