@@ -16,8 +16,8 @@
 // interleaved form is the other half of the same word.  A head is wholly in its warp's registers before
 // any of it is written, so the output may be the input.
 //
-// Bound by HBM: 16896 rows of 36 heads of 256 take 104 us, 6.1 TB/s of reading and writing each element once (94% of a
-// copy's rate); 4608 rows 30 us.  What it took: enough loads in flight per warp (one step at a time: 139 us) and few
+// Bound by HBM: 16896 rows of 36 heads of 256 take 105 us, 6.1 TB/s of reading and writing each element once (93% of a
+// copy's rate); 4608 rows 31 us.  What it took: enough loads in flight per warp (one step at a time: 139 us) and few
 // instructions per element (tables and gamma in registers for all heads of a row, fp32 in pairs).
 #pragma once
 
@@ -25,7 +25,7 @@
 
 namespace nvfp4 {
 
-constexpr int kRopeFlight = 6;  // warp steps (of 256 / D heads) in flight together
+constexpr int kRopeFlight = 6;  // warp steps (of 256 / D heads) in flight together, a multiple of 3
 
 struct RopeHeads {
   const __nv_bfloat16* x;
@@ -179,27 +179,35 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const RopeArgs a) {
     return make_uint4(r[0], r[1], r[2], r[3]);
   };
   while (true) {
-    uint32_t wide = 0u;  // steps whose head's squares leave fp32 (elements from about 1e18 on)
+    // three steps at a time: their squares, one look whether they left fp32 (at all six 3% slower with pairs as neighbours,
+    // at each step on its own 4 to 8%), their outputs
 #pragma unroll
-    for (int i = 0; i < kRopeFlight; ++i) {
-      float rstd = 1.0f;
-      if (h.gamma) {
-        rstd = rsqrtf(__fmaf_rn(head_squares<kLanes>(v[i]), 1.0f / D, a.eps));
-        if (!(rstd > 0.0f)) wide |= 1u << i;
+    for (int i0 = 0; i0 < kRopeFlight; i0 += 3) {
+      float rstd[3], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        rstd[i] = 1.0f;
+        if (h.gamma) {
+          const float ss = head_squares<kLanes>(v[i0 + i]);
+          top = fmaxf(top, ss);
+          rstd[i] = rsqrtf(__fmaf_rn(ss, 1.0f / D, a.eps));
+        }
       }
-      const uint4 r = turn(v[i], rstd);
-      if (rstd > 0.0f && head + i * kHeads < head_end) *reinterpret_cast<uint4*>(op + i * o_step) = r;
-    }
-    if (__any_sync(0xFFFFFFFFu, wide != 0u)) {
-      // those, not written yet: read again and taken down by 2^70, beside which eps is nothing
-#pragma unroll 1
-      for (int i = 0; i < kRopeFlight; ++i) {
-        const bool mine = (wide >> i & 1u) != 0u && head + i * kHeads < head_end;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (mine) u = *reinterpret_cast<const uint4*>(xp + i * x_step);
-        u = make_uint4(down70(u.x), down70(u.y), down70(u.z), down70(u.w));
-        const uint4 r = turn(u, rsqrtf(head_squares<kLanes>(u) * (1.0f / D)));
-        if (mine) *reinterpret_cast<uint4*>(op + i * o_step) = r;
+      if (__any_sync(0xFFFFFFFFu, top == INFINITY)) {
+        // elements from about 1e18 on: the head is taken down by 2^70, beside which eps is nothing
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          uint4& u = v[i0 + i];
+          const bool wide = rstd[i] == 0.0f;
+          if (wide) u = make_uint4(down70(u.x), down70(u.y), down70(u.z), down70(u.w));
+          const float ss = head_squares<kLanes>(u);
+          if (wide) rstd[i] = rsqrtf(ss * (1.0f / D));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint4 r = turn(v[i0 + i], rstd[i]);
+        if (head + (i0 + i) * kHeads < head_end) *reinterpret_cast<uint4*>(op + (i0 + i) * o_step) = r;
       }
     }
     head += kRopeFlight * kHeads;
