@@ -208,10 +208,15 @@ nvfp4_status nvfp4_cross_attention(const nvfp4_attention_desc* d, nvfp4_stream_t
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // Tiles of 128 rows, one per CTA with the keys split over clusters while there is room; or the persistent kernels' pieces
   // of two tiles.  The latter need less time for two tiles than the former for two in turn, but more than for one:
-  // a piece takes 1.25 to 1.5 times as long as a tile on its CTA (head_dim 128, 1941 keys: 38 and 25 us), and on a CTA
-  // pair (head_dim 256) 0.85 times (30 and 35 us).  So the rounds of both are compared: 1280 rows x 18 heads of 128
-  // and 1941 keys, 90 pieces or 180 tiles: 38.8 us in pieces, 48.2 in tiles; 3 samples of 600 rows, 162 or 270: 73 and 50 us;
-  // of 256: 90 pieces 56 us, 180 tiles 68 us; 162 pieces 96 us, 270 tiles 72 us.
+  // a piece takes 1.1 to 1.5 times as long as a tile on its CTA (head_dim 128: 64 keys 10.7 and 9.5 us, 512 keys 16.4 and 12.9,
+  // 1941 keys 40.7 and 26.9), and on a CTA pair (head_dim 256) 0.9 to 1 times (64 keys 12.9 and 13.2, 1941 keys 33.4 and 38.1).
+  // So the rounds of both are compared.  Pieces and tiles, inputs larger than L2 in all:
+  //   18 heads of 128: 1280 rows (1 round of pieces, 2 of tiles) 128 keys 10.5 and 15.8 us, 1941 keys 40.8 and 49.7;
+  //     3 samples of 600 (2, 2) 15.8 and 16.6, 76 and 50; 2560 (2, 3) 16.4 and 23.3, 77 and 74; 4096 (2, 4) 16.6 and 30.6, 77 and 99;
+  //   24 heads of 64: 1280 (1, 2) 128 keys 8.5 and 12.5, 1941 keys 31.8 and 45.0; 3 x 600 (2, 3) 12.1 and 17.9, 58 and 66;
+  //     4096 (3, 6) 15.8 and 32.5, 85 and 129;
+  //   18 heads of 256, rounds of pairs: 1280 (2, 2) 128 keys 18.4 and 21.7, 1941 keys 57.8 and 70.9; 3 x 600 (3, 2) 23.0 and
+  //     23.3, 84 and 73.6; 4096 (4, 4) 30.3 and 43.0, 118 and 143.
   const int64_t rows_per_work = 2 * static_cast<int64_t>(a.tok_per_tile);
   const int64_t q_works = (d->q_len + rows_per_work - 1) / rows_per_work, works = q_works * d->kv_heads * d->batch;
   if (works > (int64_t(1) << 30)) return NVFP4_ERR_UNSUPPORTED_SHAPE;

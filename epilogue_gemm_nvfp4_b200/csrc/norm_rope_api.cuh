@@ -55,9 +55,10 @@ nvfp4_status nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_heads* k, int6
       return NVFP4_ERR_MISALIGNED;
   }
   if (rows == 0) return NVFP4_OK;
-  // A warp has kRopeFlight steps of a row's heads, or, with rows enough for 24 warps per SM, all of them, which saves the
-  // reads of tables and gamma (18 heads of 256 for q and k: 37 rows 3.5 and 6.6 us, 2400 rows 17.2 and 17.0, 4608 rows
-  // 34.4 and 32.8, 16896 rows 112 and 103).
+  // A warp has kRopeFlight steps of a row's heads, or, from 24 rows per SM on, all of them, which saves the reads of tables and
+  // gamma.  18 heads of 256 for q and k, inputs larger than L2 in all, steps against all heads.  Pairs of halves: 37 rows 3.3
+  // and 6.5 us, 2400 rows 20.4 and 21.3, 2816 rows 23.8 and 23.5, 3552 rows 28.4 and 25.5, 4608 rows 35.2 and 33.5, 16896 rows
+  // 115 and 105.  Neighbours: 37 rows 3.1 and 6.2, 2400 rows 18.2 and 20.8, and within 3% either way from 3552 rows on.
   const RopeHeads few_q = rope_heads(q, head_dim, kRopeFlight), few_k = rope_heads(k, head_dim, kRopeFlight);
   if (rows > (int64_t(1) << 31) / (static_cast<int64_t>(few_q.chunks) + few_k.chunks)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
   DeviceState* st;

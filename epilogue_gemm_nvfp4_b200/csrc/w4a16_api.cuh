@@ -158,9 +158,11 @@ nvfp4_status nvfp4_w4a16_linear(const void* x, int64_t M, int64_t ldx, int32_t s
   CUtensorMap map;
   if (nvfp4_status e = make_code_map(&map, w)) return e;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // One or two rows: a CTA makes the digits of the chunks in its range for itself, if that is less work than another launch
-  // (one row of 13 chunks, N = 27648, K = 4608: 12.5 us, with the launch 13.2; two rows 14.1 and 13.2; two of 2 chunks,
-  // N = K = 4608: 8.5 and 10.1).
+  // One or two rows: a CTA makes the digits of the chunks in its range for itself, if that is less work than another launch.
+  // Weights that are not in L2, own digits against a kernel's.  One row: [4608 x 256] (1 chunk) 5.0 and 5.6 us, [4608 x 4608]
+  // (3) 7.9 and 9.3, [27648 x 4608] (14) 17.2 and 19.2, [32768 x 4608] (16) 19.6 and 21.5, [4608 x 29952] (15) 20.2 and 20.7.
+  // Two rows: [13824 x 4608] (7) 12.9 and 13.8, [4608 x 13824] (7) 14.4 and 14.4, [4608 x 18432] (9) 16.4 and 15.5, [27648 x
+  // 4608] (14) 19.7 and 19.4.
   const bool fused = M <= kW4FusedRows && M * std::min<int64_t>(a.chunks, a.base + 1) <= kW4FusedChunks;
   switch (w4_rows(M)) {
     case 2:
