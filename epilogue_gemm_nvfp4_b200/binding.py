@@ -404,8 +404,7 @@ def w4a16_linear(x: torch.Tensor, w: QTensor, kind: str = "bias", bias=None, sil
     _require(w.codes, "w.codes", torch.uint8, dev, (N, K // 2))
     _require(w.scales, "w.scales", torch.uint8, dev)
     _require(w.g, "w.g", torch.float32, dev)
-    if w.scales.numel() < 512 * (-(-N // 128) * -(-K // 64)) or not w.scales.is_contiguous() or (
-            N > 1 and w.codes.stride(0) < K // 2):
+    if w.scales.dim() != 1 or w.scales.numel() < 512 * (-(-N // 128) * -(-K // 64)) or (N > 1 and w.codes.stride(0) < K // 2):
         raise ValueError("w: rows of codes that do not overlap, and the scale bytes of its rows and columns")
     M = x.shape[0]
     n_out = N // 2 if kind == "gated_silu" else N
