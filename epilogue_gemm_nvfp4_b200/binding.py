@@ -380,7 +380,7 @@ def _raw_stream(t: torch.Tensor) -> int:
 
 def _require(t, what, dtype, device, shape=None):
     """Argument check: ``dtype``, on CUDA device number ``device``, unit stride along the last dimension, ``shape``."""
-    if t is None or t.dtype is not dtype or t.get_device() != device or (t.stride(-1) != 1 and t.shape[-1] > 1) or (
+    if t is None or t.dtype is not dtype or t.get_device() != device or (t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1) or (
             shape is not None and t.shape != shape):
         raise ValueError(f"{what}: {dtype} on one CUDA device with the call's other tensors"
                          + (f", shape {tuple(shape)}" if shape is not None else "")

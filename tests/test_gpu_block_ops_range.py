@@ -133,3 +133,16 @@ def test_few_row_linear_refuses_a_weight_smaller_than_it_says():
               B.QTensor(q.codes.view(-1), q.scales, q.g, 256, 128), B.QTensor(q.codes, q.scales[::2], q.g, 256, 128)):
         with pytest.raises(ValueError):
             B.w4a16_linear(x, w)
+
+
+def test_scalar_operands():
+    """A weight whose scale is a tensor without dimensions, as nvfp4_linear takes it; any other such operand is refused."""
+    q = B.quantize(torch.randn(256, 128, device="cuda").bfloat16())
+    x = torch.randn(2, 128, device="cuda").bfloat16()
+    scalar = torch.zeros((), dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(B.w4a16_linear(x, B.QTensor(q.codes, q.scales, q.g[0], 256, 128)), B.w4a16_linear(x, q))
+    for call in (lambda: B.w4a16_linear(x, q, bias=scalar), lambda: B.w4a16_linear(scalar, q), lambda: B.qk_norm_rope(scalar, None, None, None),
+                 lambda: B.qk_norm_rope(x.view(2, 2, 64), None, None, None, gamma_q=scalar),
+                 lambda: B.cross_attention(x.view(1, 2, 2, 64), scalar, scalar)):
+        with pytest.raises(ValueError):
+            call()
