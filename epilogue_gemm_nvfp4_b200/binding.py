@@ -401,11 +401,12 @@ def w4a16_linear(x: torch.Tensor, w: QTensor, kind: str = "bias", bias=None, sil
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError("x: [rows, K] with the weight's K")
     _require(x, "x", torch.bfloat16, dev)
-    _require(w.codes, "w.codes", torch.uint8, dev, (N, K // 2))
+    _require(w.codes, "w.codes", torch.uint8, dev)
     _require(w.scales, "w.scales", torch.uint8, dev)
     _require(w.g, "w.g", torch.float32, dev)
-    if w.scales.dim() != 1 or w.scales.numel() < 512 * (-(-N // 128) * -(-K // 64)) or (N > 1 and w.codes.stride(0) < K // 2):
-        raise ValueError("w: rows of codes that do not overlap, and the scale bytes of its rows and columns")
+    if w.codes.dim() != 2 or w.codes.shape[0] < N or w.codes.shape[1] < K // 2 or (N > 1 and w.codes.stride(0) < K // 2) or (
+            w.scales.numel() < 512 * (-(-N // 128) * -(-K // 64)) or not w.scales.is_contiguous()):
+        raise ValueError("w: codes [rows, cols / 2] whose rows do not overlap, and the scale bytes of its rows and columns")
     M = x.shape[0]
     n_out = N // 2 if kind == "gated_silu" else N
     if kind not in ("bias", "gated_silu", "resid_gate"):

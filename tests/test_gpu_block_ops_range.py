@@ -127,7 +127,11 @@ def test_few_row_linear_refuses_a_weight_smaller_than_it_says():
     """Codes or scale bytes of fewer rows or columns would be read past their end, and so would one row of codes for all."""
     q = B.quantize(torch.randn(256, 128, device="cuda").bfloat16())
     x = torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")
-    B.w4a16_linear(x, q)
+    want = B.w4a16_linear(x, q)
+    # larger buffers than it says are fine: the first rows of a longer weight, codes with more columns
+    assert torch.equal(B.w4a16_linear(x, B.QTensor(q.codes, q.scales, q.g, 128, 128)), want[:, :128])
+    wide = torch.cat((q.codes, q.codes), 1)
+    assert torch.equal(B.w4a16_linear(x, B.QTensor(wide, q.scales.view(2, -1), q.g, 256, 128)), want)
     for w in (B.QTensor(q.codes[:128], q.scales, q.g, 256, 128), B.QTensor(q.codes[:, :32], q.scales, q.g, 256, 128),
               B.QTensor(q.codes[:1].expand(256, 64), q.scales, q.g, 256, 128), B.QTensor(q.codes, q.scales[:1024], q.g, 256, 128),
               B.QTensor(q.codes.view(-1), q.scales, q.g, 256, 128), B.QTensor(q.codes, q.scales[::2], q.g, 256, 128)):
