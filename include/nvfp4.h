@@ -404,7 +404,8 @@ NVFP4_API nvfp4_status nvfp4_qk_norm_rope(const nvfp4_heads* q, const nvfp4_head
  * multiples of 8 elements, at least head_dim.  out must not overlap the inputs.  batch == 0 or q_len == 0
  * writes nothing.
  * Arithmetic: scores, maxima and sums in fp32; p is rounded to bf16 for its product with v; one rounding
- * of the output.  One launch, no scratch.
+ * of the output.  The maximum that p is taken to may lie up to 2^8 below the largest, so that sum_j p[j] v[j] passes
+ * through values of up to 2^8 times those of p <= 1, which have to fit fp32.  One launch, no scratch.
  */
 typedef struct {
   const void* q;

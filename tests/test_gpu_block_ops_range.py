@@ -126,7 +126,7 @@ def test_head_norm_refuses_operands_of_what_is_not_there():
 def test_few_row_linear_refuses_a_weight_smaller_than_it_says():
     """Codes or scale bytes of fewer rows or columns would be read past their end, and so would one row of codes for all."""
     q = B.quantize(torch.randn(256, 128, device="cuda").bfloat16())
-    x = torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(2, 128, device="cuda").bfloat16()
     want = B.w4a16_linear(x, q)
     # larger buffers than it says are fine: the first rows of a longer weight, codes with more columns
     assert torch.equal(B.w4a16_linear(x, B.QTensor(q.codes, q.scales, q.g, 128, 128)), want[:, :128])
